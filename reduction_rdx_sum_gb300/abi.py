@@ -557,8 +557,13 @@ def rdx_kv_attend(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, le
     return (_module or _marshal()).kv_attend(q, cache, block_table, lens, scale, max_len, out, lse, workspace, stream)
 
 
-def rdx_kv_attend_workspace_bytes(cache: KVCache, batch: int, q_heads: int, max_len: int) -> int:
-    """Bytes of the workspace an rdx_kv_attend call of these sizes needs (0: none)."""
+def rdx_kv_attend_workspace_bytes(cache: KVCache, batch: int, q_heads: int, max_len: int,
+                                  dtype: torch.dtype | None = None) -> int:
+    """Bytes of the workspace an rdx_kv_attend call of these sizes needs with a q of `dtype` (0: none).  The types need
+    different sizes; dtype None: enough for each of them."""
+    if dtype is not None and dtype not in TYPE_CODES:
+        raise TypeError(f"rdx_kv_attend_workspace_bytes: expected dtype in {tuple(TYPE_CODES)}, got {dtype}")
     pages = -(-max_len // cache.page_size)
-    return int(load().rdx_kv_attend_workspace_bytes(_KV_ATTEND_ARGS.pack(
-        *_KV_CACHE.unpack(cache.packed), *(0,) * 6, 0, 0, 0, 0, 0, batch, 0, pages, max_len, q_heads, 0, 1.0)))
+    return max(int(load().rdx_kv_attend_workspace_bytes(_KV_ATTEND_ARGS.pack(
+        *_KV_CACHE.unpack(cache.packed), *(0,) * 6, 0, 0, 0, 0, 0, batch, 0, pages, max_len, q_heads, code, 1.0)))
+        for code in (TYPE_CODES.values() if dtype is None else (TYPE_CODES[dtype],)))

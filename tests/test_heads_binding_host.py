@@ -1,0 +1,47 @@
+"""The Python side of the operators on heads, without a GPU: caches of fake CUDA tensors (shapes, types and devices, no
+memory) through the checks that come before any CUDA call."""
+import ctypes
+import warnings
+
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+from reduction_rdx_sum_gb300 import abi, build
+
+from test_heads_host import Attend, Cache
+
+TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return abi.load()
+
+
+def fake_cache(pages, page, heads, dim, dtype=torch.int8):
+    with warnings.catch_warnings(), FakeTensorMode():
+        warnings.simplefilter("ignore")  # of reading a fake tensor's address
+        return abi.KVCache.zeros(pages, page, heads, dim, dtype, "cuda")
+
+
+@pytest.mark.parametrize("q_heads,k_heads", [(1, 1), (32, 8), (10, 2), (24, 2), (64, 1)])
+@pytest.mark.parametrize("dim", [16, 64, 80, 128, 192, 256])
+def test_attend_workspace_of_each_type(lib, dim, q_heads, k_heads):
+    cache = fake_cache(5, 48, k_heads, dim)
+    for batch, max_len in ((1, 1), (8, 100), (300, 48), (3, 100000)):
+        need = {}
+        for dtype, code in TYPES.items():
+            a = Attend(cache=Cache(pages=5, page_size=48, heads=k_heads, head_dim=dim), batch=batch, q_heads=q_heads,
+                       table_pages=-(-max_len // 48), max_len=max_len, type=code, scale=1.0)
+            need[dtype] = lib.rdx_kv_attend_workspace_bytes(ctypes.byref(a))
+            assert need[dtype] > 0
+            assert abi.rdx_kv_attend_workspace_bytes(cache, batch, q_heads, max_len, dtype=dtype) == need[dtype]
+        # without a type: enough for either
+        assert abi.rdx_kv_attend_workspace_bytes(cache, batch, q_heads, max_len) == max(need.values())
+
+
+def test_attend_workspace_refuses_other_types(lib):
+    with pytest.raises(TypeError):
+        abi.rdx_kv_attend_workspace_bytes(fake_cache(5, 48, 2, 64), 8, 4, 100, dtype=torch.float16)

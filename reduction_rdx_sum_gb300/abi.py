@@ -507,6 +507,8 @@ class KVCache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4 or k.dtype not in KV_FORMATS:
             raise TypeError(f"KVCache: k must be a 4-D CUDA tensor of dtype in {tuple(KV_FORMATS)}")
+        if min(k.shape[1:]) < 1:
+            raise ValueError(f"KVCache: heads, page_size and head_dim must be at least 1, got k of shape {tuple(k.shape)}")
         for what, x, dtype, shape in (("k", k, k.dtype, k.shape), ("v", v, k.dtype, k.shape),
                                       ("k_scale", k_scale, torch.float32, k.shape[:3]),
                                       ("v_scale", v_scale, torch.float32, k.shape[:3])):

@@ -127,6 +127,7 @@ rdx_kv_cache cache_of(const char* name, PyObject* o, int* device) {
     if (fits) std::memcpy(&c, PyBytes_AS_STRING(packed), sizeof c);
     Py_DECREF(packed);
     TORCH_CHECK_TYPE(fits, name, ": not a KVCache of this library");
+    TORCH_CHECK_VALUE(c.page_size >= 1 && c.heads >= 1 && c.head_dim >= 1, name, ": a cache of no rows");
     PyObject* index = PyObject_GetAttr(o, g_index);
     if (index == nullptr) throw python_error();
     *device = int(PyLong_AsLong(index));

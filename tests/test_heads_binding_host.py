@@ -45,3 +45,11 @@ def test_attend_workspace_of_each_type(lib, dim, q_heads, k_heads):
 def test_attend_workspace_refuses_other_types(lib):
     with pytest.raises(TypeError):
         abi.rdx_kv_attend_workspace_bytes(fake_cache(5, 48, 2, 64), 8, 4, 100, dtype=torch.float16)
+
+
+@pytest.mark.parametrize("shape", [(4, 0, 2, 64), (4, 16, 0, 64), (4, 16, 2, 0), (0, 0, 2, 64)], ids=str)
+def test_caches_without_rows_in_a_page_are_refused(shape):
+    # attention divides by page_size; a cache of no pages is one that has no room yet
+    with pytest.raises(ValueError):
+        fake_cache(*shape)
+    assert fake_cache(0, 16, 2, 64).pages == 0

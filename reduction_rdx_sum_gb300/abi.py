@@ -445,7 +445,6 @@ PAIR_OPS = {
 TYPE_CODES = {torch.float32: 0, torch.bfloat16: 1}
 KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
-_KV_CACHE = struct.Struct("@PPPPqiiii")     # rdx_kv_cache
 _KV_ATTEND_ARGS = struct.Struct("@PPPPqiiii" + "Pqq" * 2 + "PPPPQ" + "qqqq" + "iif0q")
 
 _module = None
@@ -499,10 +498,11 @@ def rdx_qk_norm_rope_grad(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
 
 class KVCache:
     """A paged cache of 8-bit keys and values: codes k, v (int8 or float8_e4m3fn) [pages, heads, page_size, head_dim] and
-    float32 scales k_scale, v_scale [pages, heads, page_size].  The tensors stay the caller's; this checks them once and
-    keeps them alive."""
+    float32 scales k_scale, v_scale [pages, heads, page_size].  The tensors stay the caller's; this checks them and keeps
+    them alive.  Each call takes their addresses and shapes as they are then, so their storage may move or be given back
+    and brought in again; a call while it is away is refused.  The tensors themselves cannot be replaced."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "heads", "page_size", "head_dim", "index", "packed")
+    __slots__ = ("_tensors",)
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4 or k.dtype not in KV_FORMATS:
@@ -516,11 +516,16 @@ class KVCache:
                 raise TypeError(f"KVCache: {what} must be a {dtype} tensor on {k.device}")
             if x.shape != shape or not x.is_contiguous():
                 raise ValueError(f"KVCache: {what} must be contiguous with shape {tuple(shape)}, got {tuple(x.shape)}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page_size, self.head_dim = k.shape
-        self.index = k.get_device()
-        self.packed = _KV_CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages,
-                                     self.page_size, self.heads, self.head_dim, KV_FORMATS[k.dtype])
+        self._tensors = (k, v, k_scale, v_scale)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    pages = property(lambda self: self.k.shape[0])
+    heads = property(lambda self: self.k.shape[1])
+    page_size = property(lambda self: self.k.shape[2])
+    head_dim = property(lambda self: self.k.shape[3])
 
     @classmethod
     def zeros(cls, pages: int, page_size: int, heads: int, head_dim: int, dtype=torch.int8, device="cuda") -> "KVCache":
@@ -567,5 +572,6 @@ def rdx_kv_attend_workspace_bytes(cache: KVCache, batch: int, q_heads: int, max_
         raise TypeError(f"rdx_kv_attend_workspace_bytes: expected dtype in {tuple(TYPE_CODES)}, got {dtype}")
     pages = -(-max_len // cache.page_size)
     return max(int(load().rdx_kv_attend_workspace_bytes(_KV_ATTEND_ARGS.pack(
-        *_KV_CACHE.unpack(cache.packed), *(0,) * 6, 0, 0, 0, 0, 0, batch, 0, pages, max_len, q_heads, code, 1.0)))
+        0, 0, 0, 0, cache.pages, cache.page_size, cache.heads, cache.head_dim, KV_FORMATS[cache.k.dtype], *(0,) * 6,
+        0, 0, 0, 0, 0, batch, 0, pages, max_len, q_heads, code, 1.0)))
         for code in (TYPE_CODES.values() if dtype is None else (TYPE_CODES[dtype],)))

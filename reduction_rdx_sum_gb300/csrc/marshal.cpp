@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <cstring>
 #include <optional>
@@ -35,8 +36,7 @@ struct Library {
     PyObject* cache_type = nullptr;  // abi.KVCache
     PyObject* fail = nullptr;        // raises abi.RdxError(name, status)
 } g_lib;
-PyObject* g_packed = nullptr;        // attribute names
-PyObject* g_index = nullptr;
+PyObject* g_tensors = nullptr;       // attribute names
 PyObject* g_cuda_stream = nullptr;
 
 // The call in hand: its name for messages, device, stream and the guards that
@@ -117,22 +117,45 @@ at::Tensor workspace(const Call& c, PyObject* o, size_t need) {
     return x;
 }
 
+// One of a cache's four tensors, as it is now: a caller may have moved its
+// storage, or given it back, since the cache was made.
+char* cache_part(const char* name, const char* what, const at::Tensor& x, at::ScalarType type, int device, at::IntArrayRef shape) {
+    TORCH_CHECK_TYPE(x.is_cuda() && x.get_device() == device && x.scalar_type() == type, name, ": the KVCache's ", what,
+                     " must be a ", type, " tensor on CUDA device ", device);
+    TORCH_CHECK_VALUE(x.sizes() == shape && x.is_contiguous(), name, ": the KVCache's ", what,
+                      " must be contiguous with shape ", shape, ", got ", x.sizes());
+    const size_t need = x.numel() == 0 ? 0 : size_t(x.storage_offset() + x.numel()) * x.element_size();
+    TORCH_CHECK_VALUE(x.storage().nbytes() >= need, name, ": the memory of the KVCache's ", what, " is gone");
+    return static_cast<char*>(x.data_ptr());
+}
 rdx_kv_cache cache_of(const char* name, PyObject* o, int* device) {
     TORCH_CHECK_TYPE(o != nullptr && PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(g_lib.cache_type)), name,
                      ": cache must be a KVCache");
-    PyObject* packed = PyObject_GetAttr(o, g_packed);
-    if (packed == nullptr) throw python_error();
-    rdx_kv_cache c;
-    const bool fits = PyBytes_Check(packed) && size_t(PyBytes_GET_SIZE(packed)) == sizeof c;
-    if (fits) std::memcpy(&c, PyBytes_AS_STRING(packed), sizeof c);
-    Py_DECREF(packed);
+    PyObject* parts = PyObject_GetAttr(o, g_tensors);
+    if (parts == nullptr) throw python_error();
+    const THPObjectPtr held(parts);
+    bool fits = PyTuple_Check(parts) && PyTuple_GET_SIZE(parts) == 4;
+    for (int i = 0; fits && i < 4; ++i) fits = THPVariable_Check(PyTuple_GET_ITEM(parts, i));
     TORCH_CHECK_TYPE(fits, name, ": not a KVCache of this library");
-    TORCH_CHECK_VALUE(c.page_size >= 1 && c.heads >= 1 && c.head_dim >= 1, name, ": a cache of no rows");
-    PyObject* index = PyObject_GetAttr(o, g_index);
-    if (index == nullptr) throw python_error();
-    *device = int(PyLong_AsLong(index));
-    Py_DECREF(index);
-    if (PyErr_Occurred()) throw python_error();
+    const auto part = [&](int i) -> const at::Tensor& { return THPVariable_Unpack(PyTuple_GET_ITEM(parts, i)); };
+    const at::Tensor& k = part(0);
+    const at::ScalarType type = k.scalar_type();
+    TORCH_CHECK_TYPE(k.is_cuda() && k.dim() == 4 && (type == at::kChar || type == at::kFloat8_e4m3fn), name,
+                     ": the KVCache's k must be a 4-D CUDA tensor of 8-bit codes");
+    const at::IntArrayRef shape = k.sizes();
+    for (int i = 1; i < 4; ++i)
+        TORCH_CHECK_VALUE(shape[i] >= 1 && shape[i] <= INT32_MAX, name, ": a KVCache of shape ", shape);
+    *device = k.get_device();
+    rdx_kv_cache c = {};
+    c.k = cache_part(name, "k", k, type, *device, shape);
+    c.v = cache_part(name, "v", part(1), type, *device, shape);
+    c.k_scale = reinterpret_cast<float*>(cache_part(name, "k_scale", part(2), at::kFloat, *device, shape.slice(0, 3)));
+    c.v_scale = reinterpret_cast<float*>(cache_part(name, "v_scale", part(3), at::kFloat, *device, shape.slice(0, 3)));
+    c.pages = shape[0];
+    c.heads = int32_t(shape[1]);
+    c.page_size = int32_t(shape[2]);
+    c.head_dim = int32_t(shape[3]);
+    c.format = type == at::kChar ? RDX_KV_INT8 : RDX_KV_E4M3;
     return c;
 }
 
@@ -388,8 +411,7 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_method
 }  // namespace
 
 PyMODINIT_FUNC PyInit__marshal(void) {
-    g_packed = PyUnicode_InternFromString("packed");
-    g_index = PyUnicode_InternFromString("index");
+    g_tensors = PyUnicode_InternFromString("_tensors");
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    return g_packed && g_index && g_cuda_stream ? PyModule_Create(&g_module) : nullptr;
+    return g_tensors && g_cuda_stream ? PyModule_Create(&g_module) : nullptr;
 }

@@ -53,3 +53,35 @@ def test_caches_without_rows_in_a_page_are_refused(shape):
     with pytest.raises(ValueError):
         fake_cache(*shape)
     assert fake_cache(0, 16, 2, 64).pages == 0
+
+
+def marshalled(cache):
+    """A call's first step, which takes the cache apart; the ones after it need a GPU."""
+    abi._marshal().kv_read(cache, None, 0, None, None, None)
+
+
+def test_cache_tensors_cannot_be_replaced():
+    cache = fake_cache(4, 16, 2, 64)
+    for name in ("k", "v", "k_scale", "v_scale", "pages", "heads", "page_size", "head_dim"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
+    assert (cache.pages, cache.page_size, cache.heads, cache.head_dim) == (4, 16, 2, 64)
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale"])
+def test_caches_without_their_memory_are_refused(name):
+    # storage given back (offloading), or smaller than the tensor; a tensor of another shape
+    def changes(x):
+        yield lambda: x.untyped_storage().resize_(0)
+        yield lambda: x.untyped_storage().resize_(x.numel() * x.element_size() - 1)
+        yield lambda: x.resize_(3, *x.shape[1:])
+        yield lambda: x.transpose_(1, 2)
+        yield lambda: x.resize_(0, *x.shape[1:])
+
+    for i in range(5):
+        with warnings.catch_warnings(), FakeTensorMode():
+            warnings.simplefilter("ignore")
+            cache = abi.KVCache.zeros(4, 16, 2, 64, torch.int8, "cuda")
+            list(changes(getattr(cache, name)))[i]()
+            with pytest.raises((TypeError, ValueError), match=f"KVCache|{name}"):
+                marshalled(cache)

@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
             const int l = ahead.piece * S::kTokens + token_lane;
             bool there = l < ahead.len;
             if (there && (page < 0 || page >= cache.pages)) there = false;
-            const int row = there ? (page * cache.heads + ahead.key_head) * cache.page_size + l - page_index(l) * cache.page_size : -1;
+            const int row = there ? (page * cache.heads + ahead.key_head) * cache.page_size + (l - page_index(l) * cache.page_size) : -1;
             if (whole_tiles && cache.head_dim == kDim) {
                 // 16 tokens of one page are one run of bytes; rows past the
                 // sequence's end are copied as they are, or a tile of them not
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
 #pragma unroll
                     for (int h = 0; h < 2; ++h) s[x][t][2 * i + h] *= qscale[t][h] * ks;
             }
-        if (l0 + S::kTokens > at.len) {              // the row's last piece
+        if (at.len - l0 < S::kTokens) {              // the row's last piece
 #pragma unroll
             for (int x = 0; x < S::kTiles; ++x)
 #pragma unroll

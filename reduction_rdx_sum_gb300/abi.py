@@ -475,9 +475,41 @@ def rdx_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k
     """(q_out, k_out): the heads of q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim] (float32 or
     bfloat16) divided by their root mean square, times the float32 weights, and turned by the angles of row
     positions[t] of the float32 tables cos and sin [positions, rot_dim / 2] (None: no rotation).  q_out and k_out may
-    be q and k."""
-    return (_module or _marshal()).qk_norm_rope(q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved, q_out,
-                                                k_out, stream)
+    be q and k.  Where q, k or a weight requires a gradient, autograd gets it from rdx_qk_norm_rope_grad; a q_out or
+    k_out of the caller's is refused then, and tables that require one always are."""
+    y = (_module or _marshal()).qk_norm_rope(q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved, q_out,
+                                             k_out, stream)
+    return y if y is not NotImplemented else _followed_norm_rope(q, k, q_weight, k_weight, positions, cos, sin, eps,
+                                                                 interleaved, q_out, k_out, stream)
+
+
+def _followed_norm_rope(q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved, q_out, k_out, stream):
+    """rdx_qk_norm_rope where a tensor requires a gradient."""
+    if any(x is not None and x.requires_grad for x in (cos, sin)):
+        raise RuntimeError("rdx_qk_norm_rope: there is no gradient of the tables cos and sin; pass them detached")
+    if q_out is not None or k_out is not None:
+        raise RuntimeError("rdx_qk_norm_rope: a q_out or k_out of the caller's would lose the gradients that q, k, the "
+                           "weights or the outputs require; pass none, or call it under torch.no_grad()")
+    with torch.cuda.stream(stream):  # None: as it is
+        return _NormRope.apply(q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved)
+
+
+class _NormRope(torch.autograd.Function):
+    """rdx_qk_norm_rope for autograd."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, cos, sin)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return _marshal().qk_norm_rope(q, k, q_weight, k_weight, positions, cos, sin, eps, interleaved, None, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        # a loss's gradient may be one value for all: the rows' last dimension is contiguous here
+        dq_out, dk_out = (d if d.stride(2) == 1 else d.contiguous() for d in (dq_out, dk_out))
+        return (*rdx_qk_norm_rope_grad(dq_out, dk_out, *ctx.saved_tensors, eps=ctx.eps, interleaved=ctx.interleaved),
+                None, None, None, None, None)
 
 
 def rdx_qk_norm_rope_grad_workspace_bytes(head_dim: int) -> int:

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -15,7 +16,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
-#include <cstring>
+#include <cmath>
+#include <initializer_list>
 #include <optional>
 
 #include "rdx.h"
@@ -222,11 +224,25 @@ rdx_qk_norm_rope_args norm_args(const Call& c, PyObject* const* args, const at::
     return a;
 }
 
+// Whether autograd follows any of these (None and what is no tensor: not).
+bool followed(std::initializer_list<PyObject*> tensors) {
+    if (!at::GradMode::is_enabled()) return false;
+    for (PyObject* o : tensors)
+        if (o != nullptr && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) return true;
+    return false;
+}
+
+// NotImplemented where autograd follows an argument: abi.py has the function
+// that it calls back.
 PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const char* name = "rdx_qk_norm_rope";
     const at::Tensor& q = leading(name, "q", args[0]);
     const at::Tensor& k = leading(name, "k", args[1]);
+    if (followed({args[0], args[1], args[2], args[3], args[5], args[6], args[9], args[10]})) {
+        Py_INCREF(Py_NotImplemented);
+        return Py_NotImplemented;
+    }
     const Call c(name, q.get_device(), args[11]);
     const at::Tensor qo = result(c, "q_out", args[9], q.scalar_type(), q.sizes());
     const at::Tensor ko = result(c, "k_out", args[10], q.scalar_type(), k.sizes());

@@ -5,7 +5,7 @@ import torch
 
 from reduction_rdx_sum_gb300 import abi
 
-from test_heads_gpu import BF16, DEV, F32, attend_case
+from test_heads_gpu import BF16, DEV, F32, attend_case, qk_case, seeded
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,64 @@ def test_cache_follows_its_tensors():
         x.untyped_storage().resize_(bytes_)
         x.copy_(keep)
     assert torch.equal(abi.rdx_kv_attend(q, cache, table, n), want)
+
+
+def plain_norm_rope(x, w, pos, cos, sin, interleaved, eps):
+    n = x * w / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+    c, s = cos.double()[pos][:, None], sin.double()[pos][:, None]
+    rot = 2 * cos.shape[1]
+    a, b = (n[..., 0:rot:2], n[..., 1:rot:2]) if interleaved else (n[..., :rot // 2], n[..., rot // 2:rot])
+    y = a * c - b * s, b * c + a * s
+    y = torch.stack(y, -1).flatten(-2) if interleaved else torch.cat(y, -1)
+    return torch.cat((y, n[..., rot:]), -1)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_rope_under_autograd(dtype, interleaved):
+    q, k, wq, wk, pos, cos, sin = qk_case(37, 6, 2, 64, 32, dtype, "slice")
+    g = seeded(3)
+    dq, dk = torch.randn(q.shape, generator=g, device=DEV).to(dtype), torch.randn(k.shape, generator=g, device=DEV).to(dtype)
+    want = abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, interleaved=interleaved)
+    grads = abi.rdx_qk_norm_rope_grad(dq, dk, q, k, wq, wk, pos, cos, sin, interleaved=interleaved)
+    leaves = [x.detach().clone().requires_grad_() for x in (q, k, wq, wk)]
+    out = abi.rdx_qk_norm_rope(*leaves, pos, cos, sin, interleaved=interleaved)
+    assert all(torch.equal(a, b) and a.requires_grad for a, b in zip(out, want))
+    torch.autograd.backward(out, (dq, dk))
+    for x, grad in zip(leaves, grads):
+        assert torch.equal(x.grad, grad)
+    # the same from the formula in 64 bits; a float32 kernel's bound is 60 u of absolute terms (see test_heads_gpu.py),
+    # far below 2^-12 of the largest of a row's or column's gradients; a bfloat16 result adds half a unit, 2^-8
+    exact = [x.detach().double().requires_grad_() for x in (q, k, wq, wk)]
+    y = [plain_norm_rope(exact[i], exact[2 + i], pos, cos, sin, interleaved, 1e-6) for i in range(2)]
+    torch.autograd.backward(y, (dq.double(), dk.double()))
+    for i, (x, ref) in enumerate(zip(leaves, exact)):
+        top = ref.grad.abs().amax(-1, keepdim=True)
+        assert bool(((x.grad.double() - ref.grad).abs() <= top * (2.0 ** -8 if dtype is BF16 and i < 2 else 2.0 ** -12)).all())
+
+
+def test_norm_rope_gradients_of_some_arguments():
+    q, k, wq, wk, pos, cos, sin = qk_case(9, 4, 2, 64, 64, F32)
+    w = wq.clone().requires_grad_()
+    a, b = abi.rdx_qk_norm_rope(q, k, w, wk, pos, cos, sin)
+    (a.sum() + 2 * b.sum()).backward()  # gradients of one value for all: strides of 0
+    ones = torch.ones_like(q), torch.full_like(k, 2)
+    assert torch.equal(w.grad, abi.rdx_qk_norm_rope_grad(*ones, q, k, wq, wk, pos, cos, sin)[2])
+    # one result unused: its gradient is zeros
+    x = q.clone().requires_grad_()
+    abi.rdx_qk_norm_rope(x, k, wq, wk, pos, cos, sin)[0].backward(ones[0])
+    assert torch.equal(x.grad, abi.rdx_qk_norm_rope_grad(ones[0], 0 * ones[1], q, k, wq, wk, pos, cos, sin)[0])
+    # no rotation, and on another stream
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream(DEV))
+    x = q.clone().requires_grad_()
+    y, _ = abi.rdx_qk_norm_rope(x, k, wq, wk, None, None, None, stream=side)
+    torch.cuda.current_stream(DEV).wait_stream(side)
+    y.backward(ones[0])
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, abi.rdx_qk_norm_rope_grad(ones[0], 0 * ones[1], q, k, wq, wk, None, None, None)[0])
+    with torch.no_grad():
+        y, _ = abi.rdx_qk_norm_rope(x, k, wq, wk, pos, cos, sin, q_out=torch.empty_like(q))
+    assert not y.requires_grad
+    with pytest.raises(RuntimeError):
+        abi.rdx_qk_norm_rope(x, k, wq, wk, pos, cos, sin, q_out=torch.empty_like(q))

@@ -85,3 +85,21 @@ def test_caches_without_their_memory_are_refused(name):
             list(changes(getattr(cache, name)))[i]()
             with pytest.raises((TypeError, ValueError), match=f"KVCache|{name}"):
                 marshalled(cache)
+
+
+@pytest.mark.parametrize("given", ["q_out", "k_out", "cos", "sin"])
+def test_gradients_that_nothing_returns_are_refused(given):
+    # outputs of the caller's own, and the tables, have no place in autograd: an error, not a lost gradient
+    with warnings.catch_warnings(), FakeTensorMode():
+        warnings.simplefilter("ignore")
+        q, k = torch.empty(3, 2, 64, device="cuda"), torch.empty(3, 1, 64, device="cuda")
+        w = torch.empty(64, device="cuda").requires_grad_(given in ("q_out", "k_out"))
+        table = {"cos": torch.empty(5, 32, device="cuda"), "sin": torch.empty(5, 32, device="cuda")}
+        out = {}
+        if given in table:
+            table[given].requires_grad_()
+        else:
+            out[given] = torch.empty_like(q if given == "q_out" else k)
+        positions = torch.empty(3, dtype=torch.int64, device="cuda")
+        with pytest.raises(RuntimeError, match="rdx_qk_norm_rope: .*gradient"):
+            abi.rdx_qk_norm_rope(q, k, w, w, positions, table["cos"], table["sin"], **out)

@@ -130,17 +130,20 @@ char* cache_part(const char* name, const char* what, const at::Tensor& x, at::Sc
     TORCH_CHECK_VALUE(x.storage().nbytes() >= need, name, ": the memory of the KVCache's ", what, " is gone");
     return static_cast<char*>(x.data_ptr());
 }
-rdx_kv_cache cache_of(const char* name, PyObject* o, int* device) {
+struct CacheTensors {
+    THPObjectPtr held;  // the tuple of them
+    const at::Tensor& operator[](int i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(held.get(), i)); }
+};
+rdx_kv_cache cache_of(const char* name, PyObject* o, int* device, CacheTensors& x) {
     TORCH_CHECK_TYPE(o != nullptr && PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(g_lib.cache_type)), name,
                      ": cache must be a KVCache");
-    PyObject* parts = PyObject_GetAttr(o, g_tensors);
+    x.held = PyObject_GetAttr(o, g_tensors);
+    PyObject* const parts = x.held.get();
     if (parts == nullptr) throw python_error();
-    const THPObjectPtr held(parts);
     bool fits = PyTuple_Check(parts) && PyTuple_GET_SIZE(parts) == 4;
     for (int i = 0; fits && i < 4; ++i) fits = THPVariable_Check(PyTuple_GET_ITEM(parts, i));
     TORCH_CHECK_TYPE(fits, name, ": not a KVCache of this library");
-    const auto part = [&](int i) -> const at::Tensor& { return THPVariable_Unpack(PyTuple_GET_ITEM(parts, i)); };
-    const at::Tensor& k = part(0);
+    const at::Tensor& k = x[0];
     const at::ScalarType type = k.scalar_type();
     TORCH_CHECK_TYPE(k.is_cuda() && k.dim() == 4 && (type == at::kChar || type == at::kFloat8_e4m3fn), name,
                      ": the KVCache's k must be a 4-D CUDA tensor of 8-bit codes");
@@ -150,15 +153,24 @@ rdx_kv_cache cache_of(const char* name, PyObject* o, int* device) {
     *device = k.get_device();
     rdx_kv_cache c = {};
     c.k = cache_part(name, "k", k, type, *device, shape);
-    c.v = cache_part(name, "v", part(1), type, *device, shape);
-    c.k_scale = reinterpret_cast<float*>(cache_part(name, "k_scale", part(2), at::kFloat, *device, shape.slice(0, 3)));
-    c.v_scale = reinterpret_cast<float*>(cache_part(name, "v_scale", part(3), at::kFloat, *device, shape.slice(0, 3)));
+    c.v = cache_part(name, "v", x[1], type, *device, shape);
+    c.k_scale = reinterpret_cast<float*>(cache_part(name, "k_scale", x[2], at::kFloat, *device, shape.slice(0, 3)));
+    c.v_scale = reinterpret_cast<float*>(cache_part(name, "v_scale", x[3], at::kFloat, *device, shape.slice(0, 3)));
     c.pages = shape[0];
     c.heads = int32_t(shape[1]);
     c.page_size = int32_t(shape[2]);
     c.head_dim = int32_t(shape[3]);
     c.format = type == at::kChar ? RDX_KV_INT8 : RDX_KV_E4M3;
     return c;
+}
+
+// The call writes into this tensor of the caller's: operations that saved it
+// for their gradients are told.
+void written(const at::Tensor& x) {
+    if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject* o) {
+    if (!absent(o)) written(THPVariable_Unpack(o));
 }
 
 template <class Args>
@@ -247,7 +259,10 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t) {
     const at::Tensor qo = result(c, "q_out", args[9], q.scalar_type(), q.sizes());
     const at::Tensor ko = result(c, "k_out", args[10], q.scalar_type(), k.sizes());
     const rdx_qk_norm_rope_args a = norm_args(c, args, q, k, "q_out", qo, "k_out", ko);
-    return launched(c, g_lib.norm, a) ? wrapped(qo, ko) : nullptr;
+    if (!launched(c, g_lib.norm, a)) return nullptr;
+    written(args[9]);
+    written(args[10]);
+    return wrapped(qo, ko);
     END_HANDLE_TH_ERRORS
 }
 
@@ -277,6 +292,7 @@ PyObject* qk_norm_rope_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
     a.workspace = ws.data_ptr();
     a.workspace_bytes = ws.nbytes();
     if (!launched(c, g_lib.norm_grad, a)) return nullptr;
+    for (int i = 11; i < 15; ++i) written(args[i]);
     PyObject* out[4] = {THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dw[0]), THPVariable_Wrap(dw[1])};
     PyObject* t = out[0] && out[1] && out[2] && out[3] ? PyTuple_Pack(4, out[0], out[1], out[2], out[3]) : nullptr;
     for (PyObject* o : out) Py_XDECREF(o);
@@ -290,7 +306,8 @@ PyObject* kv_write(PyObject*, PyObject* const* args, Py_ssize_t) {
     const char* name = "rdx_kv_write";
     int device = 0;
     rdx_kv_rows_args a = {};
-    a.cache = cache_of(name, args[0], &device);
+    CacheTensors cache;
+    a.cache = cache_of(name, args[0], &device, cache);
     const at::Tensor& k = leading(name, "k", args[1]);
     const Call c(name, device, args[4]);
     const int64_t shape[3] = {k.size(0), a.cache.heads, a.cache.head_dim};
@@ -300,6 +317,7 @@ PyObject* kv_write(PyObject*, PyObject* const* args, Py_ssize_t) {
     a.tokens = shape[0];
     a.type = type_code(k);
     if (!launched(c, g_lib.write, a)) return nullptr;
+    for (int i = 0; i < 4; ++i) written(cache[i]);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -310,7 +328,8 @@ PyObject* kv_read(PyObject*, PyObject* const* args, Py_ssize_t) {
     const char* name = "rdx_kv_read";
     int device = 0;
     rdx_kv_rows_args a = {};
-    a.cache = cache_of(name, args[0], &device);
+    CacheTensors cache;
+    a.cache = cache_of(name, args[0], &device, cache);
     const Call c(name, device, args[5]);
     const at::Tensor& slots = tensor(name, "slots", args[1]);
     TORCH_CHECK_VALUE(slots.dim() == 1, name, ": slots must have one dimension");
@@ -322,7 +341,10 @@ PyObject* kv_read(PyObject*, PyObject* const* args, Py_ssize_t) {
     a.slots = plain<int64_t>(c, "slots", args[1], at::kLong, {shape[0]});
     a.tokens = shape[0];
     a.type = type_code(k);
-    return launched(c, g_lib.read, a) ? wrapped(k, v) : nullptr;
+    if (!launched(c, g_lib.read, a)) return nullptr;
+    written(args[3]);
+    written(args[4]);
+    return wrapped(k, v);
     END_HANDLE_TH_ERRORS
 }
 
@@ -333,7 +355,8 @@ PyObject* kv_attend(PyObject*, PyObject* const* args, Py_ssize_t) {
     int device = 0;
     const at::Tensor& q = leading(name, "q", args[0]);
     rdx_kv_attend_args a = {};
-    a.cache = cache_of(name, args[1], &device);
+    CacheTensors cache;
+    a.cache = cache_of(name, args[1], &device, cache);
     const Call c(name, device, args[9]);
     const int64_t batch = q.size(0), heads = q.size(1), dim = q.size(2);
     TORCH_CHECK_VALUE(dim == a.cache.head_dim, name, ": q has head_dim ", dim, ", the cache ", a.cache.head_dim);
@@ -364,7 +387,10 @@ PyObject* kv_attend(PyObject*, PyObject* const* args, Py_ssize_t) {
         a.workspace = ws.data_ptr();
         a.workspace_bytes = ws.nbytes();
     }
-    return launched(c, g_lib.attend, a) ? THPVariable_Wrap(out) : nullptr;
+    if (!launched(c, g_lib.attend, a)) return nullptr;
+    written(args[6]);
+    written(args[7]);
+    return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
 

@@ -120,3 +120,34 @@ def test_norm_rope_gradients_of_some_arguments():
     assert not y.requires_grad
     with pytest.raises(RuntimeError):
         abi.rdx_qk_norm_rope(x, k, wq, wk, pos, cos, sin, q_out=torch.empty_like(q))
+
+
+def test_calls_that_write_into_tensors_tell_autograd():
+    q, k, wq, wk, pos, cos, sin = qk_case(9, 4, 2, 64, 64, F32)
+    _, cache, table, n = attend_case([9, 3], 4, 2, 64, 16, "int8", F32)
+
+    def moves(call, *written):
+        before = [x._version for x in written]
+        call()
+        assert all(x._version > b for x, b in zip(written, before))
+
+    a, b, c, d = (torch.empty_like(x) for x in (q, k, wq, wk))
+    moves(lambda: abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=a, k_out=b), a, b)
+    moves(lambda: abi.rdx_qk_norm_rope_grad(q, k, q, k, wq, wk, pos, cos, sin, dq=a, dk=b, dq_weight=c, dk_weight=d), a, b, c, d)
+    slots = torch.arange(9, device=DEV)
+    moves(lambda: abi.rdx_kv_write(cache, k, k, slots), cache.k, cache.v, cache.k_scale, cache.v_scale)
+    e = torch.empty_like(b)
+    moves(lambda: abi.rdx_kv_read(cache, slots, dtype=F32, k_out=b, v_out=e), b, e)
+    out, lse = torch.empty_like(q[:2]), torch.empty(2, 4, device=DEV)
+    moves(lambda: abi.rdx_kv_attend(q[:2], cache, table, n, out=out, lse=lse), out, lse)
+    # an operation that saved q for its gradient notices
+    w = torch.ones_like(q).requires_grad_()
+    loss = (q * w).sum()
+    abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=q, k_out=k)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # tensors of inference mode have no counter
+    with torch.inference_mode():
+        a = torch.empty_like(q)
+        abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=a, k_out=k)
+    abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=a, k_out=k)

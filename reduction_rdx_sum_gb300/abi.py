@@ -447,6 +447,9 @@ KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 _KV_ATTEND_ARGS = struct.Struct("@PPPPqiiii" + "Pqq" * 2 + "PPPPQ" + "qqqq" + "iif0q")
 
+MARSHALLED = ("rdx_qk_norm_rope", "rdx_qk_norm_rope_grad", "rdx_qk_norm_rope_grad_workspace_bytes", "rdx_kv_write",
+              "rdx_kv_read", "rdx_kv_attend", "rdx_kv_attend_workspace_bytes")  # in bind's order
+
 _module = None
 
 
@@ -460,9 +463,7 @@ def _marshal():
         except ImportError as e:
             raise RuntimeError("the marshalling module is not built; run reduction_rdx_sum_gb300.build.build() "
                                f"(or __graft_entry__.build()) first ({e})") from e
-        address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "rdx_qk_norm_rope", "rdx_qk_norm_rope_grad", "rdx_qk_norm_rope_grad_workspace_bytes", "rdx_kv_write",
-            "rdx_kv_read", "rdx_kv_attend", "rdx_kv_attend_workspace_bytes")]
+        address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in MARSHALLED]
         module.bind(*address, KVCache, _check)
         _module = module
     return _module

@@ -175,7 +175,10 @@ void written(PyObject* o) {
 
 template <class Args>
 bool launched(const Call& c, Entry<Args> entry, const Args& args) {
-    const rdx_status st = entry(&args, c.stream);
+    rdx_status st;
+    Py_BEGIN_ALLOW_THREADS  // a launch waits where the queue before it is full
+    st = entry(&args, c.stream);
+    Py_END_ALLOW_THREADS
     if (st == RDX_OK) return true;
     PyObject* r = PyObject_CallFunction(g_lib.fail, "si", c.name, int(st));
     Py_XDECREF(r);

@@ -1,5 +1,10 @@
 """What the Python side of the operators on heads promises its callers: workspaces of the stated size, caches whose
 tensors move, gradients through autograd, results that other threads and streams do not disturb."""
+import ctypes
+import os
+import subprocess
+import threading
+
 import pytest
 import torch
 
@@ -151,3 +156,47 @@ def test_calls_that_write_into_tensors_tell_autograd():
         a = torch.empty_like(q)
         abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=a, k_out=k)
     abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, q_out=a, k_out=k)
+
+
+SLOW = """
+#include <stdatomic.h>
+#include <time.h>
+static atomic_int entered, left;
+int times_entered(void) { return entered; }
+int times_left(void) { return left; }
+int slow(const void* args, void* stream) {
+    const struct timespec t = {0, 300000000};
+    (void)args, (void)stream;
+    atomic_fetch_add(&entered, 1);
+    nanosleep(&t, 0);
+    atomic_fetch_add(&left, 1);
+    return 0;
+}
+"""
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    # a launch waits where the queue before it is full; a stand-in for the library's entry waits 0.3 s
+    (tmp_path / "slow.c").write_text(SLOW)
+    subprocess.run([os.environ.get("CC", "gcc"), "-O1", "-shared", "-fPIC", str(tmp_path / "slow.c"), "-o",
+                    str(tmp_path / "slow.so")], check=True)
+    slow = ctypes.CDLL(str(tmp_path / "slow.so"))
+    cache = abi.KVCache.zeros(1, 16, 2, 64, torch.int8, DEV)
+    k, slots = torch.zeros(3, 2, 64, device=DEV), torch.arange(3, device=DEV)
+    abi.rdx_kv_write(cache, k, k, slots)
+    entries = [ctypes.cast(getattr(abi.load(), name), ctypes.c_void_p).value for name in abi.MARSHALLED]
+    stand_in = ctypes.cast(slow.slow, ctypes.c_void_p).value
+    module = abi._marshal()
+    module.bind(*(stand_in if name == "rdx_kv_write" else e for name, e in zip(abi.MARSHALLED, entries)), abi.KVCache,
+                abi._check)
+    try:
+        caller = threading.Thread(target=abi.rdx_kv_write, args=(cache, k, k, slots))
+        caller.start()
+        while slow.times_entered() == 0 and caller.is_alive():
+            pass
+        inside = slow.times_entered() == 1 and slow.times_left() == 0  # this thread runs, and the call is not back yet
+        caller.join()
+    finally:
+        module.bind(*entries, abi.KVCache, abi._check)
+    assert inside
+    abi.rdx_kv_write(cache, k, k, slots)

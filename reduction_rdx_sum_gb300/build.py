@@ -6,7 +6,8 @@ runtime (the one PyTorch has already loaded, when it has).  ptxas resource
 usage (registers, spills, shared memory) is written to ``_build/ptxas.txt``.
 Nothing is rebuilt while the library is newer than every source and header.
 ``_marshal.so`` (csrc/marshal.cpp, g++ against PyTorch's headers) marshals the
-arguments of the calls over heads; it is compiled alongside.
+arguments of the calls over heads from Python; it is compiled alongside where
+PyTorch is installed.
 
     python -m reduction_rdx_sum_gb300.build [--force] [-DNAME=VALUE ...]
 """
@@ -61,13 +62,22 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _torch_dir() -> str | None:
+    """PyTorch's folder; None without PyTorch, or with one that has no CUDA."""
+    spec = importlib.util.find_spec("torch")
+    path = spec.submodule_search_locations[0] if spec is not None else ""
+    return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
 def build_marshal(force: bool = False) -> str:
     """Compile the marshalling extension module; returns its path."""
     src = os.path.join(CSRC, "marshal.cpp")
     inputs = [src, os.path.join(INCLUDE, "rdx.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
         return MARSHAL
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        raise RuntimeError("the marshalling module needs PyTorch with CUDA, which is not installed")
     include = os.path.join(torch_dir, "include")
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", include,
@@ -82,9 +92,12 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, defines: list[str] | None = None, out: str = LIB, verbose: bool = False) -> str:
-    """Compile and link librdx.so; returns its path."""
+    """Compile and link librdx.so; returns its path.  The in-tree library's marshalling module, too, where PyTorch is
+    installed: C programs need neither."""
+    if out != LIB or _torch_dir() is None:
+        return _build_library(force, defines, out, verbose)
     with ThreadPoolExecutor(1) as ex:
-        marshal = ex.submit(build_marshal, force and out == LIB)
+        marshal = ex.submit(build_marshal, force)
         path = _build_library(force, defines, out, verbose)
         marshal.result()
     return path

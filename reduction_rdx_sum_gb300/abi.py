@@ -463,6 +463,10 @@ def _marshal():
         except ImportError as e:
             raise RuntimeError("the marshalling module is not built; run reduction_rdx_sum_gb300.build.build() "
                                f"(or __graft_entry__.build()) first ({e})") from e
+        built_for = getattr(module, "torch_version", "another version")
+        if built_for != torch.__version__:
+            raise RuntimeError(f"the marshalling module was built for PyTorch {built_for}, this is "
+                               f"{torch.__version__}; run reduction_rdx_sum_gb300.build.build() again")
         address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in MARSHALLED]
         module.bind(*address, KVCache, _check)
         _module = module

@@ -16,6 +16,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -69,18 +70,28 @@ def _torch_dir() -> str | None:
     return path if os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
 
 
+def torch_version() -> str:
+    """The installed PyTorch's version, read without importing it."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+
+
 def build_marshal(force: bool = False) -> str:
-    """Compile the marshalling extension module; returns its path."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    inputs = [src, os.path.join(INCLUDE, "rdx.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
-        return MARSHAL
+    """Compile the marshalling extension module; returns its path.  It is bound to the PyTorch and the Python that it was
+    compiled for, which a note in _build/ names: for others it is compiled again."""
     torch_dir = _torch_dir()
     if torch_dir is None:
         raise RuntimeError("the marshalling module needs PyTorch with CUDA, which is not installed")
+    src, note = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.txt")
+    fits = f"PyTorch {torch_version()} in {torch_dir}, Python {sys.version}"
+    inputs = [src, os.path.join(INCLUDE, "rdx.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
+        if os.path.exists(note) and open(note).read() == fits:
+            return MARSHAL
     include = os.path.join(torch_dir, "include")
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", include,
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f'-DRDX_TORCH_VERSION="{torch_version()}"', "-I", INCLUDE, "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_path("include"),
            "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include"), src, "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
@@ -88,6 +99,9 @@ def build_marshal(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, MARSHAL)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(note, "w") as f:
+        f.write(fits)
     return MARSHAL
 
 

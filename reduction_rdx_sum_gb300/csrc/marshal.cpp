@@ -458,5 +458,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_method
 PyMODINIT_FUNC PyInit__marshal(void) {
     g_tensors = PyUnicode_InternFromString("_tensors");
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    return g_tensors && g_cuda_stream ? PyModule_Create(&g_module) : nullptr;
+    PyObject* m = g_tensors && g_cuda_stream ? PyModule_Create(&g_module) : nullptr;
+    // abi.py compares it: the module reads tensors through this version's headers
+    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", RDX_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
 }

@@ -44,3 +44,24 @@ def test_builds_into_another_path_are_the_library_alone(compiles, tmp_path):
     assert compiles and marshal_compiles(compiles) == 0
     build.build(force=True, out=build.LIB)
     assert marshal_compiles(compiles) == 1
+
+
+def test_the_module_is_rebuilt_for_another_pytorch(compiles, monkeypatch):
+    build.build_marshal()
+    build.build_marshal()
+    assert marshal_compiles(compiles) == 1  # up to date
+    monkeypatch.setattr(build, "torch_version", lambda: "0.0.1")
+    build.build_marshal()
+    build.build_marshal()
+    assert marshal_compiles(compiles) == 2
+
+
+def test_a_module_of_another_pytorch_is_not_used(monkeypatch):
+    build.build()
+    assert build.torch_version() == torch.__version__
+    monkeypatch.setattr(abi, "_module", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(RuntimeError, match="0.0.1"):
+        abi._marshal()
+    monkeypatch.undo()
+    assert abi._marshal().torch_version == torch.__version__

@@ -27,18 +27,22 @@
 //
 // Rounding.  q is divided by a power of two (its row's maximum becomes 2^7 to
 // 2^8) and rounded to half precision: for a bfloat16 q that is exact down to 2^-32
-// of the row's maximum; a float32 one takes two parts (22 bits).  Weights
-// exp(s - m) vscale keep float32's range, as a channel's only nonzero codes may
-// belong to tokens of tiny weight: they are split into bfloat16 parts, two (16
-// bits) where the result is a bfloat16, of 8 bits itself, three (24 bits) where
-// it is a float32.  Sums are float32.  The
-// matrix instructions drop what an addition shifts out instead of rounding it:
-// about 2^-25 of the sum each time, always towards 0.  For float32 results each
-// step's products therefore start from 0, smallest parts first, and are added
-// by ordinary rounded additions (the error against 64 bits of 35936 tokens went
-// from 3.4e-6 to 4.7e-7; plain float32 arithmetic gives 1.4e-6); for bfloat16
-// results the loss would reach a quarter of their rounding after 8192 pieces of
-// one warp, a cache of 120 GB.
+// of the row's maximum; a float32 one takes two parts (22 bits; the result's
+// error, 1.3e-7 at up to 2047 tokens of 64, is plain float32's, 1.2e-7).  Weights exp(s - m) vscale are
+// split into three bfloat16 parts, float32's 24 bits and its range, as a
+// channel's only nonzero codes may belong to tokens of tiny weight (two parts
+// would be up to 9 % faster where instructions are the bound, 9 to 16 query heads
+// a key head or head_dim 64, and 1 to 3 % where memory is).  Sums are float32.
+// The matrix instructions drop what an addition shifts out instead of rounding
+// it: about 2^-25 of the sum each time, always towards 0.  So a step's products
+// start from 0, smallest parts first, and are added by ordinary rounded
+// additions: in float32, the error against 64 bits of 35936 tokens went from
+// 3.4e-6 to 4.7e-7 (plain float32 arithmetic gives 1.4e-6); in bfloat16, the loss
+// was 2e-6 of the values over 128 pieces of one warp and 0.5 %, more than the
+// result's rounding, after 27 thousand (2^31 tokens of head_dim 16); it costs 1 %
+// there, 5 % for 256 values or 16 heads.  Two sums of bfloat16 calls stay in
+// the instructions, being short: a score's 4 to 16 steps, and a cluster's weighted
+// sums, as its warps have at most 24 steps each.
 //
 // Split.  A row of work is one sequence, key head and block of 8 or 16 of its
 // query heads; its tokens are cut into pieces of 32 (16 for the widest rows).
@@ -53,8 +57,8 @@
 // a block's warps first, then the cluster's blocks; so one launch (cluster_of).
 //
 // Measured (bfloat16 q, 32 + 8 heads of 128): 4 sequences of 131071 tokens, e4m3,
-// 170-172 us, 6.5 TB/s of cache; 64 uneven ones up to 8192 tokens, int8, 72 us
-// (4.9 TB/s), of which the join is 5; without the arithmetic the copies alone
+// 172-174 us, 6.4 TB/s of cache; 64 uneven ones up to 8192 tokens, int8, 73 us
+// (4.8 TB/s), of which the join is 5; without the arithmetic the copies alone
 // take 56.  Cutting each sequence into chunks of one block instead took 200 and
 // 100 us: a block's start and end cost about 4 us, and uneven lengths left SMs
 // idle.  One sequence of 4099 tokens takes 11 us in clusters of 16 blocks: a warp
@@ -122,6 +126,12 @@ __device__ __forceinline__ void matrix_step_bf16(float (&d)[4], const uint32_t (
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// a += x and b += y in one instruction, each rounded.
+__device__ __forceinline__ void add_two(float& a, float& b, float x, float y) {
+    asm("{\n.reg .b64 s, t;\nmov.b64 s, {%0, %1};\nmov.b64 t, {%2, %3};\nadd.rn.f32x2 s, s, t;\nmov.b64 {%0, %1}, s;\n}"
+        : "+f"(a), "+f"(b)
+        : "f"(x), "f"(y));
 }
 // An 8x8 matrix of 16-bit values, a row's pair a lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -338,20 +348,23 @@ struct Joined {
 
 // Blocks of an SM, as its shared memory and registers allow.  More blocks hide
 // more of each other's latency, until the accumulators spill: 16 sequences of
-// 16384 tokens take, at 16 query heads a key head, 141 us with two blocks of
-// 255 registers and 185 us with three of 168; in float32 114 us and 131 us.
+// 16384 tokens on 8 key heads of 128 take, at 16 query heads a key head, 155 us
+// with two blocks of 255 registers and 207 us with three of 168; in float32, at
+// 4 query heads, 108 us and 115 us.
 constexpr int blocks_per_sm(size_t type_bytes, int dim, int tiles) {
     return dim == 64 ? (tiles == 1 ? 4 : 3) : dim == 128 && type_bytes == 2 && tiles == 1 ? 3 : 2;
 }
 
 // T: the type of q and out; kDim: head_dim rounded up to 64, 128 or 256 (the
-// rest is zeros); kTiles: tiles of 8 query heads.
-template <class T, int kFormat, int kDim, int kTiles>
+// rest is zeros); kTiles: tiles of 8 query heads; kClustered: a cluster of
+// blocks for each row, not runs of the line.
+template <class T, int kFormat, int kDim, int kTiles, bool kClustered>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTiles))
     kv_attend_kernel(const __grid_constant__ AttendParams p) {
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr int kWeightParts = kParts + 1;
-    constexpr bool kFresh = kParts == 2;             // sums of a step added by themselves
+    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;   // of a query
+    constexpr int kWeightParts = 3;
+    constexpr bool kFreshScores = kParts == 2;       // a step's products added by rounded additions
+    constexpr bool kFreshSums = kParts == 2 || !kClustered;
     constexpr int kSteps = kDim / 16;                // of the scores' product
     constexpr int kRowChunks = kDim / 16;
     constexpr int kOutTiles = kDim / 16;             // of 16 values of out^T
@@ -373,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
     const int index = blockIdx.x * kWarps + warp;
     Place at;
     int64_t last;
-    if (p.cluster > 0) {                             // an equal share of one row
+    if constexpr (kClustered) {                      // an equal share of one row
         __syncthreads();                             // the zeros
         const int row = blockIdx.x / p.cluster, share = index - row * p.cluster * kWarps, shares = p.cluster * kWarps;
         at.b = row / p.rows;
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
                     widen4<kFormat>(wh[j], a[1], a[3]);
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
-                        if constexpr (kFresh) {
+                        if constexpr (kFreshScores) {
                             matrix_step_half(run[t], a, q[t][0][4 * i + j]);
                             if constexpr (kParts == 2) matrix_step_half(low[t], a, q[t][1][4 * i + j]);
                         } else {
@@ -670,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
                         }
                     }
                 }
-                if constexpr (kFresh)
+                if constexpr (kFreshScores)
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -778,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
 #pragma unroll
                         for (int t = 0; t < kTiles; ++t) {
                             float(&sum)[4] = acc[t][(u * kWords + j) * 2 + half];
-                            if constexpr (kFresh) {
+                            if constexpr (kFreshSums) {
                                 float fresh[4] = {};
 #pragma unroll
                                 for (int part = kWeightParts - 1; part >= 0; --part) matrix_step_bf16(fresh, a, w[t][part]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) sum[i] += fresh[i];
+                                add_two(sum[0], sum[1], fresh[0], fresh[1]);
+                                add_two(sum[2], sum[3], fresh[2], fresh[3]);
                             } else {
 #pragma unroll
                                 for (int part = 0; part < kWeightParts; ++part) matrix_step_bf16(sum, a, w[t][part]);
@@ -794,14 +807,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T), kDim, kTile
         }
 
         begins = at.piece + 1 == at.pieces;
-        if (p.cluster == 0 && (begins || at.unit + 1 == last)) {  // the part's end
+        if (!kClustered && (begins || at.unit + 1 == last)) {  // the part's end
             const int64_t part = (index + at.b * p.rows + at.row) * p.block_heads;
             leave(p.sums + part * cache.head_dim, p.stats + part, false);
         }
         step(at);
     }
     copies_wait<0>();
-    if (p.cluster == 0) return;
+    if (!kClustered) return;
 
     // ---- the row's parts joined, four values a thread: the block's warps, then the cluster's blocks
     constexpr int kPart = kTiles * 8 * (kDim + 2);   // words of a part: sums, then the statistics
@@ -1025,17 +1038,17 @@ Layout layout_of(const KvAttendPlan& p, const Split& s) {
 
 // Blocks of a row's cluster, 0 for the line.  Where every row can have a cluster
 // at once and a warp's share stays short, one kernel is faster than two: of 32
-// query heads on 8 key heads of 128, one sequence of 512 tokens takes 7.8 us
-// against 9.8, one of 4096 10.5 against 11.5, 16 of 500 11.7 against 13.4 (and
+// query heads on 8 key heads of 128, one sequence of 512 tokens takes 7.4 us
+// against 10.2, one of 4096 10.3 against 12.0, 16 of 500 11.6 against 13.8 (and
 // on the host 6 us against 9).  From there on the line's even shares and full
-// SMs count for more: 8 sequences of 2000 tokens (four pieces a warp) 16.7
-// against 16.3, 16 uneven ones up to 1000 (four) 13.4 against 11.6; with 12 heads
-// of 64, 16 up to 1000 (four) 12.1 against 9.7, up to 500 (two) 8.1 against 8.7;
-// with 4 key heads of 256, 32 of 1000 (eight pieces of 16) 24.3 against 30.1.  Up
-// to a piece a warp more blocks make a row faster (8 sequences of 500: one block
-// a row 11.1 us, two 9.6, four 9.5), then no more; nor beyond four results a
-// thread when they are joined (16 query heads a key head, 8 sequences of 64
-// tokens: one block 12.9, four 10.9).
+// SMs count for as much or more: 8 sequences of 2000 tokens (four pieces a warp)
+// 16.2 either way, 16 uneven ones up to 1000 (four) 13.4 against 12.2; with 12
+// heads of 64, 16 up to 1000 (four) 11.8 against 10.0, up to 500 (two) 7.9
+// against 9.0; with 4 key heads of 256, 32 of 1000 (eight pieces of 16) 22.6
+// against 23.7.  Up to a piece a warp more blocks make a row faster (8 sequences
+// of 500: one block a row 11.1 us, two 9.4, four 9.4), then no more; nor beyond
+// four results a thread when they are joined (16 query heads a key head, 8
+// sequences of 64 tokens: one block 13.2, four 11.8).
 template <int kDim>
 int cluster_of(const AttendParams& a) {
     constexpr int64_t kTokens = Stage<kDim>::kTokens, kMost = kDim == 64 ? 2 : kDim == 128 ? 3 : 8;  // pieces a warp
@@ -1054,19 +1067,23 @@ cudaError_t join(const AttendParams& a, cudaStream_t stream) {
                       dim3(kJoinWarps<kSplit> * kWarpSize), stream, a);
 }
 
+template <class T, int kFormat, int kDim, int kTiles, bool kClustered>
+cudaError_t start(bool early, unsigned blocks, const AttendParams& a, cudaStream_t stream) {
+    const auto kernel = kv_attend_kernel<T, kFormat, kDim, kTiles, kClustered>;
+    constexpr size_t kSmem = kWarps * kRing * sizeof(Stage<kDim>);
+    static SharedMemoryGrant grant;
+    const cudaError_t e = grant.ask(kernel, kSmem, kClustered);
+    return e != cudaSuccess ? e : launch_smem(early, kernel, dim3(blocks), dim3(kThreads), kSmem, stream,
+                                              kClustered ? unsigned(a.cluster) : 1u, a);
+}
+
 template <class T, int kFormat, int kDim, int kTiles>
 cudaError_t launch(AttendParams a, cudaStream_t stream) {
-    const auto kernel = kv_attend_kernel<T, kFormat, kDim, kTiles>;
-    constexpr size_t kSmem = kWarps * kRing * sizeof(Stage<kDim>);
     constexpr int kTokens = Stage<kDim>::kTokens;
-    static SharedMemoryGrant grant;
-    cudaError_t e = grant.ask(kernel, kSmem, true);
-    if (e != cudaSuccess) return e;
     a.cluster = cluster_of<kDim>(a);
     if (a.cluster > 0) {
         const unsigned blocks = unsigned(a.batch * a.rows * a.cluster);
-        return launch_smem(blocks < unsigned(a.warps / kWarps), kernel, dim3(blocks), dim3(kThreads), kSmem, stream,
-                           unsigned(a.cluster), a);
+        return start<T, kFormat, kDim, kTiles, true>(blocks < unsigned(a.warps / kWarps), blocks, a, stream);
     }
     // no more blocks than the longest lengths could use
     const __int128 most = __int128(a.batch) * a.rows * (kRowUnits + (int64_t(a.max_len) + kTokens - 1) / kTokens);
@@ -1077,11 +1094,12 @@ cudaError_t launch(AttendParams a, cudaStream_t stream) {
     // of its memory, and with it room for fewer of these (64 uneven sequences up
     // to 8192 tokens, one call after the other: 93 us instead of 75).
     const bool early = grid < unsigned(a.warps / kWarps);
-    e = launch_smem(early, kernel, dim3(grid), dim3(kThreads), kSmem, stream, 1u, a);
+    const cudaError_t e = start<T, kFormat, kDim, kTiles, false>(early, grid, a, stream);
     if (e != cudaSuccess) return e;
     // The fewer heads there are, the more parts each has: 16 warps for each of up
-    // to one head an SM (6 heads of 340 parts: 13.8 us for the call, 16.3 with 8
-    // warps), 4 for a few a SM (512 heads: 97.4 us; with 16, 106), else 2.
+    // to one head an SM (6 heads on one sequence of 16384 tokens: 15.0 us for the
+    // call, 16.7 with 8 warps), 4 for a few a SM (512 heads of 64 uneven
+    // sequences: 69.1 us; with 16, 77.7), else 2 (2048 heads: 72.5; with 4, 75.5).
     const int64_t heads = a.batch * a.q_heads;
     return heads <= 152 ? join<T, kTokens, 16>(a, stream)
                         : heads <= 1024 ? join<T, kTokens, 4>(a, stream) : join<T, kTokens, 2>(a, stream);

@@ -7,7 +7,7 @@ import torch
 
 from reduction_rdx_sum_gb300 import abi
 
-from test_heads_gpu import DEV, F32, FORMATS, seeded
+from test_heads_gpu import BF16, DEV, F32, FORMATS, attend_case, check_attend, make_rows, seeded
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,21 @@ def test_sums_that_grow_and_cancel(fmt):
     bound = 2.0 ** -20 * v.abs().mean(0) + 2.0 ** -8 * ref.abs()
     off = (out[0].double() - ref).abs() / bound
     assert float(off.max()) <= 1, float(off.max())
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("case", [([300, 17, 0], 8, 2, 64, 16), ([90, 200], 12, 1, 128, 48), ([33], 5, 5, 80, 7),
+                                  ([77, 1], 6, 2, 256, 32)], ids=str)
+def test_bfloat16_rows_of_every_layout(case, fmt):
+    # rows read and written value by value, or four at a time, are the same rows
+    lens, hq, hk, dim, page = case
+    q, cache, table, n = attend_case(lens, hq, hk, dim, page, fmt, BF16)
+    for wide, longest in both_ways(table, page, max(lens)):
+        lse = torch.empty(len(lens), hq, device=DEV)
+        want = abi.rdx_kv_attend(q, cache, wide, n, lse=lse, max_len=longest)
+        check_attend(want, lse, q, cache, wide, n, dim ** -0.5, BF16)
+        for layout in ("slice", "heads", "off"):
+            x = make_rows(seeded(1), len(lens), hq, dim, BF16, layout).copy_(q)
+            y = make_rows(seeded(2), len(lens), hq, dim, BF16, layout)
+            abi.rdx_kv_attend(x, cache, wide, n, out=y, max_len=longest)
+            assert torch.equal(y, want), layout

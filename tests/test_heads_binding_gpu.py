@@ -200,3 +200,43 @@ def test_other_threads_run_while_a_call_waits(tmp_path):
         module.bind(*entries, abi.KVCache, abi._check)
     assert inside
     abi.rdx_kv_write(cache, k, k, slots)
+
+
+def test_threads_and_streams_do_not_disturb_each_other():
+    # four threads, each on a stream of its own with sizes of its own, through every operator; each result as alone
+    def work(i, stream):
+        q, k, wq, wk, pos, cos, sin = qk_case(50 + 300 * i, 8, 2, 64, 64, (F32, BF16)[i % 2], seed=i)
+        x, cache, table, n = attend_case([200 + 900 * i, 31], 8, 2, 64, 16, "int8", (F32, BF16)[i % 2], seed=i)
+        slots = torch.arange(q.shape[0], device=DEV)
+        fresh = abi.KVCache.zeros(-(-q.shape[0] // 16), 16, 2, 64, torch.int8, DEV)
+        torch.cuda.current_stream(DEV).synchronize()
+
+        def once():
+            a, b = abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin, stream=stream)
+            grads = abi.rdx_qk_norm_rope_grad(q, k, q, k, wq, wk, pos, cos, sin, stream=stream)
+            abi.rdx_kv_write(fresh, k, b, slots, stream=stream)
+            back = abi.rdx_kv_read(fresh, slots, dtype=F32, stream=stream)
+            return (a, b, *grads, *back, abi.rdx_kv_attend(x, cache, table, n, stream=stream))
+
+        return once
+
+    streams = [torch.cuda.Stream(DEV) for _ in range(4)]
+    calls = [work(i, s) for i, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    alone = [c() for c in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        for _ in range(20):
+            got = calls[i]()
+            streams[i].synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

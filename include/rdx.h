@@ -413,7 +413,9 @@ rdx_status rdx_sum_f32_noalloc(const float* x, int64_t n, float* out, cudaStream
  *  - Arguments come in a struct of plain values, read before the call
  *    returns; a zeroed struct is a valid start.
  *  - Values are float32 or bfloat16 (RDX_TYPE_*); sums, statistics and
- *    products accumulate in float32 and each result is rounded once.
+ *    products accumulate in float32 and each result is rounded once.  (In
+ *    rdx_kv_attend a float32 q enters the products with 22 bits, each row
+ *    relative to its maximum.)
  *  - Results are the same bits from run to run, for the same sizes, strides,
  *    alignment and lengths.
  *  - A call enqueues one kernel; rdx_qk_norm_rope_grad, whose partial sums are
@@ -454,6 +456,8 @@ typedef struct rdx_heads {
  *   positions    tokens int64 values;  cos, sin  [max_pos][rot_dim / 2]
  *                float32 (all three ignored when rot_dim == 0); a position
  *                outside [0, max_pos) makes the token's rotated values NaN
+ *   A row whose sum of squares passes float32's range (values of 2^59 and more
+ *   may) gives zeros.
  *   q_out, k_out may be q and k themselves (same address and strides);
  *                otherwise no output may overlap an input or the other output
  * Errors: RDX_ERR_INVALID_ARG for anything outside the above, NULL or
@@ -580,7 +584,8 @@ rdx_status rdx_kv_read(const rdx_kv_rows_args* args, cudaStream_t stream);
  *   lse          [batch][q_heads] float32, or NULL
  *   workspace    rdx_kv_attend_workspace_bytes(args) bytes (0: none needed),
  *                16-byte aligned
- * The order of the sums depends on the sizes, max_len and lens.  Magnitudes of 2^100 and more may overflow in the weighted sums.
+ * The order of the sums depends on the sizes, max_len and lens.  Magnitudes
+ * of 2^100 and more may overflow in the weighted sums.
  * Errors: RDX_ERR_INVALID_ARG for anything outside the above.
  */
 typedef struct rdx_kv_attend_args {

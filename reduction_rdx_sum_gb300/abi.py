@@ -595,9 +595,9 @@ def rdx_kv_attend(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, le
     """out [batch, q_heads, head_dim]: attention of one query token a sequence, q (float32 or bfloat16), over the first
     lens[b] (int32) tokens of the cache's pages block_table[b] (int32 [batch, pages]).  scale: default head_dim ** -0.5.
     max_len: no length is above it (default: all the table's pages; a close bound lets few, short sequences take a
-    faster way).  lse: a float32 [batch, q_heads] tensor that receives
-    the logarithm of each softmax sum.  A sequence of length 0 gives zeros (lse -inf); a length outside [0, max_len] or a
-    page outside the cache gives NaN."""
+    faster way).  lse: a float32 [batch, q_heads] tensor that receives the logarithm of each softmax sum.  A sequence of
+    length 0 gives zeros (lse -inf); a length outside [0, max_len] or a page outside the cache gives NaN.  The result is
+    detached, like a reduction's: this operator, the cache's write and its read have no gradients."""
     return (_module or _marshal()).kv_attend(q, cache, block_table, lens, scale, max_len, out, lse, workspace, stream)
 
 

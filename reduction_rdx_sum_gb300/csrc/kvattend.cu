@@ -28,21 +28,21 @@
 // Rounding.  q is divided by a power of two (its row's maximum becomes 2^7 to
 // 2^8) and rounded to half precision: for a bfloat16 q that is exact down to 2^-32
 // of the row's maximum; a float32 one takes two parts (22 bits; the result's
-// error, 1.3e-7 at up to 2047 tokens of 64, is plain float32's, 1.2e-7).  Weights exp(s - m) vscale are
-// split into three bfloat16 parts, float32's 24 bits and its range, as a
-// channel's only nonzero codes may belong to tokens of tiny weight (two parts
-// would be up to 9 % faster where instructions are the bound, 9 to 16 query heads
-// a key head or head_dim 64, and 1 to 3 % where memory is).  Sums are float32.
-// The matrix instructions drop what an addition shifts out instead of rounding
-// it: about 2^-25 of the sum each time, always towards 0.  So a step's products
-// start from 0, smallest parts first, and are added by ordinary rounded
+// error, 1.3e-7 at up to 2047 tokens of 64, is plain float32's, 1.2e-7).  Weights
+// exp(s - m) vscale are split into three bfloat16 parts, float32's 24 bits and its
+// range, as a channel's only nonzero codes may belong to tokens of tiny weight
+// (two parts would be up to 9 % faster where instructions are the bound, 9 to 16
+// query heads a key head or head_dim 64, and 1 to 3 % where memory is).  Sums are
+// float32.  The matrix instructions drop what an addition shifts out instead of
+// rounding it: about 2^-25 of the sum each time, always towards 0.  So a step's
+// products start from 0, smallest parts first, and are added by ordinary rounded
 // additions: in float32, the error against 64 bits of 35936 tokens went from
 // 3.4e-6 to 4.7e-7 (plain float32 arithmetic gives 1.4e-6); in bfloat16, the loss
 // was 2e-6 of the values over 128 pieces of one warp and 0.5 %, more than the
-// result's rounding, after 27 thousand (2^31 tokens of head_dim 16); it costs 1 %
-// there, 5 % for 256 values or 16 heads.  Two sums of bfloat16 calls stay in
-// the instructions, being short: a score's 4 to 16 steps, and a cluster's weighted
-// sums, as its warps have at most 24 steps each.
+// result's rounding, after 27 thousand (2^31 tokens of head_dim 16); the additions
+// cost 2 %, and 5 to 8 for rows of 256 values or 16 heads.  Two sums of bfloat16
+// calls stay in the instructions, being short: a score's 4 to 16 steps, and a
+// cluster's weighted sums, as its warps have at most 24 steps each.
 //
 // Split.  A row of work is one sequence, key head and block of 8 or 16 of its
 // query heads; its tokens are cut into pieces of 32 (16 for the widest rows).
@@ -57,7 +57,7 @@
 // a block's warps first, then the cluster's blocks; so one launch (cluster_of).
 //
 // Measured (bfloat16 q, 32 + 8 heads of 128): 4 sequences of 131071 tokens, e4m3,
-// 172-174 us, 6.4 TB/s of cache; 64 uneven ones up to 8192 tokens, int8, 73 us
+// 172-175 us, 6.4 TB/s of cache; 64 uneven ones up to 8192 tokens, int8, 73 us
 // (4.8 TB/s), of which the join is 5; without the arithmetic the copies alone
 // take 56.  Cutting each sequence into chunks of one block instead took 200 and
 // 100 us: a block's start and end cost about 4 us, and uneven lengths left SMs
@@ -149,7 +149,8 @@ __device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float
 template <int kFormat>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (kFormat == RDX_KV_INT8) {
-        // 0x64uu is the 16-bit float 1024 + u; u = code + 128
+        // the usual conversion by a fixed exponent: 0x64uu is the 16-bit float
+        // 1024 + u, whose last bit is 1; u = code + 128
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = __floats2half2_rn(1152.f, 1152.f);
         uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
@@ -1156,7 +1157,8 @@ cudaError_t kv_attend_launch(const KvAttendPlan& plan, cudaStream_t stream) {
     };
     a.wide_q = wide(plan.q);
     a.wide_out = wide(plan.out);
-    // for l < 2^31: shift s = ceil(log2 d), magic = floor(2^32 (2^s - d) / d) + 1
+    // Division by an invariant d (Granlund and Montgomery, 1994), for l < 2^31:
+    // shift s = ceil(log2 d), magic = floor(2^32 (2^s - d) / d) + 1
     while (int64_t(1) << a.page_shift < plan.cache.page_size) ++a.page_shift;
     a.page_magic = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << a.page_shift) - plan.cache.page_size)) / plan.cache.page_size + 1);
     if (plan.type == RDX_TYPE_BF16)

@@ -240,3 +240,15 @@ def test_threads_and_streams_do_not_disturb_each_other():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_rope_rows_past_the_range(dtype):
+    # squares that pass float32's range: the row is zeros, as in plain float32 arithmetic; its neighbours are untouched
+    q, k, wq, wk, pos, cos, sin = qk_case(5, 4, 2, 64, 64, dtype)
+    want = abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin)
+    q[2, 1] = 2.0 ** 70
+    got = abi.rdx_qk_norm_rope(q, k, wq, wk, pos, cos, sin)
+    assert not got[0][2, 1].any()
+    got[0][2, 1] = want[0][2, 1]
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
